@@ -133,6 +133,22 @@ __device__ __forceinline__ uint4 inside_bits(int lo, int hi) {
 __device__ __forceinline__ uint4 and4(const uint4 &a, const uint4 &b) {
     return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
 }
+__device__ __forceinline__ uint4 select4(const uint4 &m, const uint4 &a, uint32_t b) {
+    return make_uint4((a.x & m.x) | (b & ~m.x), (a.y & m.y) | (b & ~m.y),
+                      (a.z & m.z) | (b & ~m.z), (a.w & m.w) | (b & ~m.w));
+}
+// A value of T in every place of a word.
+template <typename T>
+__device__ __forceinline__ uint32_t spread(float v) {
+    if constexpr (Vec<T>::E == 4) {
+        return __float_as_uint(v);
+    } else {
+        const T e = from_f32<T>(v);
+        uint16_t h;
+        memcpy(&h, &e, 2);
+        return h * 0x10001u;
+    }
+}
 __device__ __forceinline__ f32x2 inside_pair(int q, int lo, int hi) {
     return pair(2 * q >= lo && 2 * q < hi ? 1.f : 0.f,
                 2 * q + 1 >= lo && 2 * q + 1 < hi ? 1.f : 0.f);
@@ -207,6 +223,32 @@ struct RowSpan {
     // zeros outside the row
     __device__ __forceinline__ uint4 only(int i, const uint4 &v) const {
         return edge(i) ? and4(v, inside_bits<T>(lo(i), hi(i))) : v;
+    }
+    // one of the vector's own elements of the row in the places outside it: the
+    // last in the row's first vector, else the first (V > 1: the row goes on past
+    // its first vector)
+    __device__ __forceinline__ uint4 only_own(int i, const uint4 &v) const {
+        static_assert(V > 1, "a row in one vector may end before its last element");
+        if (!edge(i)) return v;
+        const bool start = i == 0 && t == 0 && first;
+        const uint32_t w = start ? v.w : v.x;
+        return select4(inside_bits<T>(lo(i), hi(i)), v,
+                       E == 4 ? w : __byte_perm(w, 0u, start ? 0x3232u : 0x1010u));
+    }
+    // `fill` there
+    __device__ __forceinline__ uint4 only_or(int i, const uint4 &v, uint32_t fill) const {
+        return edge(i) ? select4(inside_bits<T>(lo(i), hi(i)), v, fill) : v;
+    }
+    __device__ __forceinline__ void only_or(int i, f32x2 (&d)[E / 2], float fill) const {
+        if (edge(i)) {
+#pragma unroll
+            for (int q = 0; q < E / 2; ++q) {
+                float a, b;
+                split(d[q], a, b);
+                d[q] = pair(2 * q >= lo(i) && 2 * q < hi(i) ? a : fill,
+                            2 * q + 1 >= lo(i) && 2 * q + 1 < hi(i) ? b : fill);
+            }
+        }
     }
     __device__ __forceinline__ void only(int i, f32x2 (&d)[E / 2]) const {
         if (edge(i)) {
@@ -451,6 +493,8 @@ ln_bwd_ragged_kernel(T *__restrict__ dresid, const T *__restrict__ dout,
             } else if constexpr (L > 32) {
                 m_next = to_f32(inp[rr * C]);              // the pivot
             }
+        } else {
+            m_next = s_next = 0.f;                         // no row: xhat is zero below
         }
         copy_commit();
     };
@@ -479,31 +523,35 @@ ln_bwd_ragged_kernel(T *__restrict__ dresid, const T *__restrict__ dout,
         fetch(r + rstep, stage ^ 1);
         copy_wait<1>();
         const uint4 *xs = s_st + stage * NS * NVM, *ds = xs + NVM, *ps = ds + NVM;
-        // Element pairs of vector i.  Nothing of a neighbour's row may enter a
-        // sum (0 * infinity): zeros outside the row.
+        // Vector i.  Nothing of a neighbour's row may enter a sum (0 * infinity):
+        // zeros outside the row, or for x the pivot.
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         auto vec = [&](const uint4 *from, int i) {
-            return valid ? row.only(i, from[row.j(i)]) : make_uint4(0u, 0u, 0u, 0u);
+            return valid ? row.only(i, from[row.j(i)]) : zero;
         };
+        uint32_t fill = 0u;
+        auto vec_p = [&](int i) { return valid ? row.only_or(i, xs[row.j(i)], fill) : zero; };
+        float k = m;                                       // K as a number
         f32x2 K = pair(m, m), MD = pair(0.f, 0.f);
         if constexpr (RECOMP) {
             float pivot;
             if constexpr (L <= 32)
-                pivot = __shfl_sync(0xffffffffu, row.in(0) ? element_of<T>(vec(xs, 0), row.sh) : 0.f,
+                pivot = __shfl_sync(0xffffffffu,
+                                    valid && row.in(0) ? element_of<T>(xs[row.j(0)], row.sh) : 0.f,
                                     lane & ~(L - 1));
             else
                 pivot = m;
+            k = pivot;
             K = pair(pivot, pivot);
+            fill = spread<T>(pivot);
             f32x2 sd = pair(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 if (row.in(i)) {
                     f32x2 x[P];
-                    to_pairs<T>(vec(xs, i), x);
+                    to_pairs<T>(vec_p(i), x);
 #pragma unroll
-                    for (int q = 0; q < P; ++q) x[q] = sub2(x[q], K);
-                    row.only(i, x);
-#pragma unroll
-                    for (int q = 0; q < P; ++q) sd = add2(sd, x[q]);
+                    for (int q = 0; q < P; ++q) sd = add2(sd, sub2(x[q], K));
                 }
             }
             const float md =
@@ -515,7 +563,7 @@ ln_bwd_ragged_kernel(T *__restrict__ dresid, const T *__restrict__ dout,
             for (int i = 0; i < V; ++i) {
                 if (row.in(i)) {
                     f32x2 x[P];
-                    to_pairs<T>(vec(xs, i), x);
+                    to_pairs<T>(vec_p(i), x);
 #pragma unroll
                     for (int q = 0; q < P; ++q) x[q] = sub2(sub2(x[q], K), MD);
                     row.only(i, x);
@@ -534,13 +582,32 @@ ln_bwd_ragged_kernel(T *__restrict__ dresid, const T *__restrict__ dout,
             if constexpr (RECOMP) d = sub2(d, MD);
             return mul2(d, S);
         };
-        // outside the row dout is zero, so those elements add nothing here
+        // Outside the row dout is zero, and xhat must be finite for its product
+        // with dout to be zero too.  For x = 0 it is -mean * rstd, which overflows
+        // for a row of the type's lowest value (3.4e38 * 316).  So x there is one
+        // of the vector's own elements, or, where a lane's one vector may hold the
+        // whole row, K in the rows that need it; with recomputed statistics the
+        // pivot, selected as bits or, with several warps a row, as numbers.
+        // Measured on B200: the plain zeros 67.2 us at bf16 24001 x 1023, own
+        // elements 68.0, K selected in every row 72.5; recomputed 8000 x 5001 as
+        // numbers 122 against 147 as bits, 24001 x 1023 98 against 90.
+        [[maybe_unused]] const bool far = !(fabsf(m * s) <= 3.402823466e38f);
         f32x2 s1 = pair(0.f, 0.f), s2 = pair(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             if (row.in(i)) {
                 f32x2 x[P], dy[P], wp[P];
-                to_pairs<T>(vec(xs, i), x);
+                if constexpr (!RECOMP && V > 1) {
+                    to_pairs<T>(valid ? row.only_own(i, xs[row.j(i)]) : zero, x);
+                } else if constexpr (!RECOMP) {
+                    to_pairs<T>(vec(xs, i), x);
+                    if (far) row.only_or(i, x, k);
+                } else if constexpr (L > 64) {
+                    to_pairs<T>(xs[row.j(i)], x);
+                    row.only_or(i, x, k);
+                } else {
+                    to_pairs<T>(vec_p(i), x);
+                }
                 to_pairs<T>(vec(ds, i), dy);
                 smem_pairs<P>(s_w + row.j(i) * E, wp);
 #pragma unroll

@@ -1,0 +1,117 @@
+"""The dropout operators on a B200 where values leave the ordinary range:
+infinities and NaN beside finite rows and in dropped places of the gradient,
+rows of the type's largest values, and a weight array off a 16-byte boundary.
+
+The comparisons are exact wherever the definition gives an exact answer: a row
+is a function of its own inputs, so a run with non-finite values in some rows
+must leave the others' bits as a run without them does, and a dropped place of
+dbranch is zero whatever stands in dx."""
+import numpy as np
+import pytest
+import torch
+
+import dropout_ref as dr
+import gpu_util as gu
+import oracle
+import tolerances as tol
+
+pytestmark = pytest.mark.gpu
+
+RECOMPUTE = 4
+SEED, OFFSET, P, EPS = 99, 1 << 33, 0.25, 1e-5
+
+# rows of several per warp, whole vectors and not, one warp, several warps, the
+# rings, the split ring, past them (16 bits) and past the ragged kernels
+WIDTHS = [12, 64, 601, 768, 1024, 1031, 1600, 2048, 6145, 8193, 12296]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return gu.ln()
+
+
+def _rows(C, many):
+    """Few rows: the one-launch backward where there is one; many: a grid that
+    takes several turns where the rows are short, the last with groups of a
+    warp that have no row."""
+    return 7 if not many else (20009 if C <= 64 else 1203 if C <= 2048 else 67)
+
+
+def _normal(gen, shape, dtype, sigma=1.0):
+    return (torch.randn(shape, generator=gen, device="cuda") * sigma).to(gu.TORCH_DT[dtype])
+
+
+def _kept(N, C):
+    return torch.from_numpy(dr.keep(N * C, P, SEED, OFFSET).reshape(N, C)).cuda()
+
+
+def _forward(lib, dtype, resid, branch, w, b, p=P):
+    N, C = resid.shape
+    x = gu.nan_tensor((N, C), resid.dtype)
+    out, mean, rstd = gu.forward_outputs(N, C, dtype)
+    lib.ln_forward_dropout_residual(x, out, mean, rstd, resid, branch, w, b, N, C, EPS, p, SEED,
+                                    OFFSET, None, gu.DT[dtype])
+    return x, out, mean, rstd
+
+
+def _backward(lib, dtype, inp, dout, w, stats, prev, inplace=False, p=P):
+    """stats: (mean, rstd), or None to recompute them."""
+    N, C = inp.shape
+    dres, dbr = (gu.nan_tensor((N, C), inp.dtype) for _ in range(2))
+    dw, db = (gu.nan_tensor((C,), torch.float32) for _ in range(2))
+    if inplace:
+        dres.copy_(prev)
+        prev = dres
+    mean, rstd = stats or (None, None)
+    lib.ln_backward_dropout_residual(dres, dbr, dw, db, prev, dout, inp, w, mean, rstd, N, C, EPS,
+                                     p, SEED, OFFSET, None, gu.DT[dtype],
+                                     0 if stats else RECOMPUTE)
+    return dres, dbr, dw, db
+
+
+def _same_bits(name, a, b, rows=None):
+    a, b = (a, b) if rows is None else (a[rows], b[rows])
+    bad = gu.bits(a.contiguous()) != gu.bits(b.contiguous())
+    assert not bad.any(), f"{name}: {int(bad.sum())} of {bad.numel()} differ"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("many", [False, True])
+def test_rows_of_the_largest_values(lib, dtype, C, many):
+    """The odd rows (few rows: every row) a constant of the type's lowest
+    value.  x - mean is then exactly zero: out is bias, rstd 1 / sqrt(eps),
+    xhat zero, dresid and dbranch and the column sums finite and those of the
+    definition."""
+    N = _rows(C, many)
+    g = torch.Generator(device="cuda").manual_seed(5 * N + C)
+    low = torch.finfo(gu.TORCH_DT[dtype]).min
+    w, b = 1 + _normal(g, (C,), dtype, 0.1), _normal(g, (C,), dtype, 0.1)
+    resid, dout, prev = (_normal(g, (N, C), dtype) for _ in range(3))
+    resid[1::2 if many else 1] = low
+    resid[0] = low
+    branch = torch.zeros_like(resid)
+    x, out, mean, rstd = _forward(lib, dtype, resid, branch, w, b)
+    label = f"{dtype} {N}x{C}"
+    _same_bits(f"{label} x", x, resid)
+    flat = (resid == low).all(1)
+    _same_bits(f"{label} out", out[flat], b.expand(int(flat.sum()), C))
+    assert (mean[flat] == low).all(), f"{label}: mean {mean[flat][:4]}"
+    kept = dr.keep(N * C, P, SEED, OFFSET).reshape(N, C)
+    h = gu.to_f64
+    _, m64, s64 = oracle.default().forward(h(x), h(w), h(b), EPS)
+    tol.check(f"{label} rstd", h(rstd), s64, dtype, "stats")
+    m32, s32 = m64.astype(np.float32), s64.astype(np.float32)
+    for saved in (True, False):
+        stats = (torch.from_numpy(m32).cuda(), torch.from_numpy(s32).cuda()) if saved else None
+        got = _backward(lib, dtype, x, dout, w, stats, prev)
+        ref = dr.backward(h(prev), h(dout), h(x), h(w), m32, s32, EPS, kept, P, not saved)
+        sc = tol.magnitude_scales(h(x), h(dout), h(w), m64, s64)
+        up = float(dr.scale32(P))
+        for name, kind, u, v, s in zip(
+                ("dresid", "dbranch", "dweight", "dbias"),
+                ("act_bwd", "act_bwd", "param_grad", "param_grad"), got, ref,
+                (sc["dinp"], sc["dinp"] * up, sc["dweight"], sc["dbias"])):
+            assert torch.isfinite(u).all(), f"{label} {name} saved={saved}: not finite"
+            tol.check(f"{label} {name} saved={saved}", h(u), v, dtype, kind, s)
