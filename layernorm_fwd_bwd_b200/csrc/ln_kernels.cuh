@@ -57,13 +57,15 @@ constexpr int kFwdDropout = 2;
 // sums d - coarse(mean_d) into `left`, coarse() keeping 12 significant bits:
 // for 16-bit rows these differences are exact (mean_d in full would round each
 // of them the same way) and small, and so is their sum's error (3e-8 of the
-// mean).  out and rstd do not use it.
+// mean).  out and rstd do not use it.  Where the distances or their sum are not
+// finite, neither is `left` (infinity - infinity), and the mean is ln_forward's:
+// infinite for a row that holds an infinity.
 __device__ __forceinline__ float coarse(float mean_d) {
     return __uint_as_float(__float_as_uint(mean_d) & 0xfffff000u);
 }
 __device__ __forceinline__ float mean_with_rest(float pivot, float mean_d, float left,
                                                 float inv_C) {
-    return (pivot + coarse(mean_d)) + left * inv_C;
+    return isfinite(left) ? (pivot + coarse(mean_d)) + left * inv_C : pivot + mean_d;
 }
 // Backward: dinp += the gradient (the previous dinp is read and the sum is
 // rounded to T once).

@@ -115,3 +115,23 @@ def test_rows_of_the_largest_values(lib, dtype, C, many):
                 (sc["dinp"], sc["dinp"] * up, sc["dweight"], sc["dbias"])):
             assert torch.isfinite(u).all(), f"{label} {name} saved={saved}: not finite"
             tol.check(f"{label} {name} saved={saved}", h(u), v, dtype, kind, s)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("C", WIDTHS)
+def test_mean_of_a_row_with_an_infinity(lib, dtype, C):
+    """mean is the sum of the row over C: infinite where the row holds an
+    infinity of one sign (in a kept place, not the first, which is the point the
+    distances are taken from), as ln_forward gives it for the stored row."""
+    N = 6
+    g = torch.Generator(device="cuda").manual_seed(C)
+    w, b = 1 + _normal(g, (C,), dtype, 0.1), _normal(g, (C,), dtype, 0.1)
+    resid, branch = (_normal(g, (N, C), dtype) for _ in range(2))
+    resid[1, C // 2] = float("inf")
+    resid[2, C - 1] = float("-inf")
+    x, _, mean, rstd = _forward(lib, dtype, resid, branch, w, b)
+    _, m2, r2 = gu.forward(lib, x, w, b, N, C, EPS, dtype)
+    assert mean[1] == float("inf") and mean[2] == float("-inf"), mean
+    assert torch.equal(torch.isnan(mean), torch.isnan(m2))
+    assert torch.isnan(rstd[1:3]).all() and torch.isnan(r2[1:3]).all()
+    assert torch.isfinite(mean[[0, 3, 4, 5]]).all()
