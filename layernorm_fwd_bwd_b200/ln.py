@@ -168,14 +168,32 @@ def _stream(s):
     return s.cuda_stream
 
 
+# What _step compares a counter with: its element types and the query of the
+# current device, set by the first call with a tensor.
+_counter_types = ()
+_current_device = None
+
+
+def _find_counter_types():
+    global _counter_types, _current_device
+    import torch
+    _current_device = torch.cuda.current_device
+    _counter_types = (torch.int64, torch.uint64)
+
+
 def _step(x):
-    """Address of a dropout counter: one 64-bit integer in device memory.  A
-    tensor of another kind is refused here, since the kernel would read eight
-    bytes of whatever it is."""
+    """Address of a dropout counter: one 64-bit integer in the current
+    device's memory.  A tensor of another kind or of another device is refused
+    here, since the kernel would read eight bytes of whatever it is."""
     if x is None or isinstance(x, int):
         return x
-    if not x.is_cuda or x.element_size() != 8 or x.numel() < 1:
-        raise TypeError("step: a CUDA tensor of one 64-bit integer, or None")
+    if not _counter_types:
+        _find_counter_types()
+    device = x.get_device()                    # -1: the host
+    if device < 0 or x.dtype not in _counter_types or x.numel() != 1:
+        raise TypeError("step: a CUDA tensor of one 64-bit integer, a device address or None")
+    if device != _current_device():
+        raise TypeError("step: a tensor of the current device")
     return x.data_ptr()
 
 
@@ -226,8 +244,8 @@ def ln_dropout(out, inp, n: int, p: float, seed: int, offset: int, step, dtype: 
     """out <- dropout(inp) over n elements; its backward is the same call on
     the gradient.  The mask is a function of (seed, offset + step, element
     index): ``seed`` and ``offset`` are 64-bit integers (signed or unsigned),
-    ``step`` is None or a one-element 64-bit CUDA tensor (or device address)
-    that the kernel adds to ``offset`` when it runs."""
+    ``step`` is None or a CUDA tensor of one 64-bit integer (or its device
+    address) that the kernel adds to ``offset`` when it runs."""
     _check(_lib.ln_dropout(_ptr(out), _ptr(inp), int(n), float(p), int(seed), int(offset),
                            _step(step), int(dtype), _stream(stream)))
 

@@ -135,3 +135,46 @@ def test_mean_of_a_row_with_an_infinity(lib, dtype, C):
     assert torch.equal(torch.isnan(mean), torch.isnan(m2))
     assert torch.isnan(rstd[1:3]).all() and torch.isnan(r2[1:3]).all()
     assert torch.isfinite(mean[[0, 3, 4, 5]]).all()
+
+
+def _counter(kind):
+    return {"int32": lambda: torch.zeros(2, dtype=torch.int32, device="cuda"),
+            "float64": lambda: torch.ones(1, dtype=torch.float64, device="cuda"),
+            "complex64": lambda: torch.ones(1, dtype=torch.complex64, device="cuda"),
+            "two": lambda: torch.zeros(2, dtype=torch.int64, device="cuda"),
+            "none": lambda: torch.zeros(0, dtype=torch.int64, device="cuda"),
+            "host": lambda: torch.zeros(1, dtype=torch.int64)}[kind]()
+
+
+@pytest.mark.parametrize("kind", ["int32", "float64", "complex64", "two", "none", "host"])
+def test_other_counters_are_refused(lib, kind):
+    """step is one 64-bit integer of the current GPU; anything else is refused
+    by every call before a kernel runs."""
+    step = _counter(kind)
+    N, C = 4, 8
+    a = [torch.zeros(N, C, device="cuda") for _ in range(6)]
+    v = [torch.ones(C, device="cuda") for _ in range(4)]
+    n0 = lib.launch_count()
+    with pytest.raises(TypeError):
+        lib.ln_dropout(a[0], a[1], N * C, P, 0, 0, step, lib.LN_F32)
+    with pytest.raises(TypeError):
+        lib.ln_forward_dropout_residual(a[0], a[1], v[0], v[1], a[2], a[3], v[2], v[3], N, C, EPS,
+                                        P, 0, 0, step, lib.LN_F32)
+    with pytest.raises(TypeError):
+        lib.ln_backward_dropout_residual(a[0], a[1], v[0], v[1], None, a[2], a[3], v[2], v[3],
+                                         v[3], N, C, EPS, P, 0, 0, step, lib.LN_F32)
+    assert lib.launch_count() == n0
+
+
+def test_integer_counters_are_taken(lib):
+    """int64 and uint64, of one element and of any number of dimensions, an
+    element of a larger tensor too: all draw the same mask."""
+    n = 4096
+    inp = torch.ones(n, device="cuda")
+    base = torch.tensor([3, 7, 11], dtype=torch.int64, device="cuda")
+    want = dr.keep(n, P, SEED, OFFSET, 7)
+    for step in (base[1], base[1:2], base[1].reshape(1, 1), base[1:2].view(torch.uint64),
+                 base.data_ptr() + 8):
+        out = torch.empty_like(inp)
+        lib.ln_dropout(out, inp, n, P, SEED, OFFSET, step, lib.LN_F32)
+        assert np.array_equal(gu.to_f64(out) != 0, want)
