@@ -224,13 +224,17 @@ int ln_backward_ex(void *dinp, float *dweight, float *dbias, const void *dout,
  *           unscaled; T = 65536 drops every element.  Dropped elements are
  *           exactly zero, whatever value (infinity, NaN) they had.
  *   seed, offset   64-bit keys, any value (read as unsigned bit patterns).
- *           Two calls with the same keys draw the same mask: give every
- *           dropout of every step its own offset, and a backward the keys of
- *           its forward.
+ *           Two calls with the same seed and offset + *step draw the same
+ *           mask: give every dropout of every step its own sum, and a backward
+ *           the keys of its forward.
  *   step    device address of a 64-bit counter added to offset when the
  *           kernel runs, 8-byte aligned, or NULL (adds 0).  A captured CUDA
  *           graph keeps the offset it was captured with; a counter that the
- *           graph's owner advances gives every replay a new mask.
+ *           graph's owner advances gives every replay a new mask.  Dropouts
+ *           that share a seed and a counter need offsets further apart than
+ *           the counter ever runs, for example site << 32 with a counter
+ *           advanced by 1 per step: with neighbouring offsets, site s at one
+ *           step would have the mask of site s - 1 at the next.
  * These calls follow the semantics above (streams, determinism, aliasing,
  * graphs).  Every array must lie on a multiple of its element size
  * (LN_ERR_ALIGN).

@@ -245,7 +245,9 @@ def ln_dropout(out, inp, n: int, p: float, seed: int, offset: int, step, dtype: 
     the gradient.  The mask is a function of (seed, offset + step, element
     index): ``seed`` and ``offset`` are 64-bit integers (signed or unsigned),
     ``step`` is None or a CUDA tensor of one 64-bit integer (or its device
-    address) that the kernel adds to ``offset`` when it runs."""
+    address) that the kernel adds to ``offset`` when it runs.  Dropouts that
+    share a seed and a counter need offsets further apart than the counter
+    ever runs (``site << 32`` with a counter advanced by 1 per step)."""
     _check(_lib.ln_dropout(_ptr(out), _ptr(inp), int(n), float(p), int(seed), int(offset),
                            _step(step), int(dtype), _stream(stream)))
 

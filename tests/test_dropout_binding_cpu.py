@@ -1,7 +1,13 @@
 """What the binding's dropout calls take as their counter, on a host without a
-GPU: tensors are stood in for by objects that answer the same questions."""
+GPU: tensors are stood in for by objects that answer the same questions.  And
+the keys that the documentation's example gives them."""
+import os
+import re
+
 import pytest
 import torch
+
+import dropout_ref as dr
 
 
 @pytest.fixture(scope="module")
@@ -58,3 +64,19 @@ def test_counters(lib):
     assert lib._step(1 << 40) == 1 << 40
     for dtype in (torch.int64, torch.uint64):
         assert lib._step(Counter(dtype)) == 4096
+
+
+def test_documented_keys_draw_a_mask_once():
+    """README's example: over sites and steps no two dropouts have the same
+    seed and offset + step, so no mask is drawn twice."""
+    readme = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    line = re.search(r"^keys = (\(.*?\))\s+#", open(readme).read(), re.M).group(1)
+    drawn, masks = set(), set()
+    sites, steps = 25, (0, 1, 2, 3, 10 ** 6)
+    for site in range(sites):
+        for step in steps:
+            p, seed, offset, counter = eval(line, {"seed": 7, "site": site, "step": step})
+            assert counter == step and 0 < p < 1
+            drawn.add((seed, (offset + counter) % (1 << 64)))
+            masks.add(dr.keep(256, p, seed, offset, counter).tobytes())
+    assert len(drawn) == sites * len(steps) == len(masks)
