@@ -79,6 +79,80 @@ def _same_bits(name, a, b, rows=None):
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("C", WIDTHS)
 @pytest.mark.parametrize("many", [False, True])
+def test_non_finite_rows_stay_alone(lib, dtype, C, many):
+    """Infinities and NaN in three rows (resid, branch, inp or dout; with rows
+    that share a 16-byte vector with their neighbours): the other rows' results
+    are those of a run without them, bit for bit."""
+    N = _rows(C, many)
+    g = torch.Generator(device="cuda").manual_seed(N + C)
+    w, b = 1 + _normal(g, (C,), dtype, 0.1), _normal(g, (C,), dtype, 0.1)
+    resid, branch, dout, prev = (_normal(g, (N, C), dtype) for _ in range(4))
+    bad = torch.tensor([1, N // 2, N - 1], device="cuda")
+    fine = torch.ones(N, dtype=torch.bool, device="cuda")
+    fine[bad] = False
+    clean = _forward(lib, dtype, resid, branch, w, b)
+    r2, b2 = resid.clone(), branch.clone()
+    r2[bad[0]] = float("inf")
+    b2[bad[1]] = float("nan")
+    r2[bad[2], ::2] = float("-inf")
+    b2[bad[2], 1::2] = float("inf")
+    for name, u, v in zip(("x", "out", "mean", "rstd"), clean, _forward(lib, dtype, r2, b2, w, b)):
+        assert torch.isfinite(u).all()
+        _same_bits(f"{dtype} {N}x{C} {name}", u, v, fine)
+
+    x, _, mean, rstd = clean
+    for stats in ((mean, rstd), None):
+        for inplace in (False, True):
+            ref = _backward(lib, dtype, x, dout, w, stats, prev, inplace)
+            x2, d2 = x.clone(), dout.clone()
+            x2[bad[0]] = float("inf")
+            d2[bad[1]] = float("nan")
+            x2[bad[2], ::2] = float("nan")
+            d2[bad[2], 1::2] = float("-inf")
+            got = _backward(lib, dtype, x2, d2, w, stats, prev, inplace)
+            for name, u, v in zip(("dresid", "dbranch"), ref, got):
+                assert torch.isfinite(u).all()
+                _same_bits(f"{dtype} {N}x{C} {name} saved={stats is not None}", u, v, fine)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("many", [False, True])
+def test_dbranch_is_zero_where_dropped(lib, dtype, C, many):
+    """Infinities and NaN of the gradient in dropped places leave exact zeros in
+    dbranch, come through in kept places, and touch neither the other elements
+    nor dweight and dbias (dresid_out enters no sum)."""
+    N = _rows(C, many)
+    g = torch.Generator(device="cuda").manual_seed(3 * N + C)
+    w = 1 + _normal(g, (C,), dtype, 0.1)
+    x, dout, prev = (_normal(g, (N, C), dtype) for _ in range(3))
+    _, mean, rstd = gu.forward(lib, x, w, w, N, C, EPS, dtype)
+    kept = _kept(N, C)
+    p2 = prev.clone()
+    p2[:, 0::3] = float("nan")
+    p2[:, 1::3] = float("-inf")
+    hurt = torch.zeros(C, dtype=torch.bool, device="cuda")
+    hurt[0::3] = hurt[1::3] = True
+    for stats in ((mean, rstd), None):
+        for inplace in (False, True):
+            label = f"{dtype} {N}x{C} saved={stats is not None} inplace={inplace}"
+            ref = _backward(lib, dtype, x, dout, w, stats, prev, inplace)
+            dres, dbr, dw, db = _backward(lib, dtype, x, dout, w, stats, p2, inplace)
+            assert (dbr[~kept] == 0).all(), f"{label}: dropped places"
+            assert not torch.isfinite(dbr[:, hurt][kept[:, hurt]]).any(), label
+            assert not torch.isfinite(dres[:, hurt]).any(), label
+            _same_bits(f"{label} dresid", dres[:, ~hurt], ref[0][:, ~hurt])
+            _same_bits(f"{label} dbranch", dbr[:, ~hurt], ref[1][:, ~hurt])
+            _same_bits(f"{label} dweight", dw, ref[2])
+            _same_bits(f"{label} dbias", db, ref[3])
+            # a rate of one: nothing reaches the branch
+            _, none, _, _ = _backward(lib, dtype, x, dout, w, stats, p2, inplace, p=1.0)
+            assert (none == 0).all(), f"{label}: p = 1"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("many", [False, True])
 def test_rows_of_the_largest_values(lib, dtype, C, many):
     """The odd rows (few rows: every row) a constant of the type's lowest
     value.  x - mean is then exactly zero: out is bias, rstd 1 / sqrt(eps),
@@ -135,6 +209,45 @@ def test_mean_of_a_row_with_an_infinity(lib, dtype, C):
     assert torch.equal(torch.isnan(mean), torch.isnan(m2))
     assert torch.isnan(rstd[1:3]).all() and torch.isnan(r2[1:3]).all()
     assert torch.isfinite(mean[[0, 3, 4, 5]]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("many", [False, True])
+def test_weight_off_a_boundary(lib, dtype, C, many):
+    """weight and bias that start one element into an allocation, everything
+    else on 16 bytes: what aligned copies of them give, to the tolerances of
+    the two kernels that may serve the calls."""
+    N = _rows(C, many)
+    g = torch.Generator(device="cuda").manual_seed(7 * N + C)
+    w, b = 1 + _normal(g, (C + 1,), dtype, 0.1), _normal(g, (C + 1,), dtype, 0.1)
+    w, b = w[1:], b[1:]
+    assert w.data_ptr() % 16 == gu.SIZE[dtype] == b.data_ptr() % 16
+    wa, ba = w.clone(), b.clone()
+    resid, branch, dout, prev = (_normal(g, (N, C), dtype) for _ in range(4))
+    label = f"{dtype} {N}x{C}"
+    ref = _forward(lib, dtype, resid, branch, wa, ba)
+    got = _forward(lib, dtype, resid, branch, w, b)
+    _same_bits(f"{label} x", got[0], ref[0])
+    h = gu.to_f64
+    rout, m64, s64 = oracle.default().forward(h(got[0]), h(w), h(b), EPS)
+    sc = tol.magnitude_scales(h(got[0]), h(dout), h(w), m64, s64)
+    tol.check(f"{label} out", h(got[1]), rout, dtype, "act_fwd")
+    tol.check(f"{label} mean", h(got[2]), m64, dtype, "stats", sc["mean"])
+    tol.check(f"{label} rstd", h(got[3]), s64, dtype, "stats")
+    kept = dr.keep(N * C, P, SEED, OFFSET).reshape(N, C)
+    m32, s32 = m64.astype(np.float32), s64.astype(np.float32)
+    for saved in (True, False):
+        stats = (torch.from_numpy(m32).cuda(), torch.from_numpy(s32).cuda()) if saved else None
+        grads = _backward(lib, dtype, got[0], dout, w, stats, prev)
+        want = dr.backward(h(prev), h(dout), h(got[0]), h(w), m32, s32, EPS, kept, P, not saved)
+        up = float(dr.scale32(P))
+        for name, kind, u, v, s in zip(
+                ("dresid", "dbranch", "dweight", "dbias"),
+                ("act_bwd", "act_bwd", "param_grad", "param_grad"), grads, want,
+                (sc["dinp"], sc["dinp"] * up, sc["dweight"], sc["dbias"])):
+            tol.check(f"{label} {name} saved={saved}", h(u), v, dtype, kind, s)
+    assert lib.device_status() == 0
 
 
 def _counter(kind):
