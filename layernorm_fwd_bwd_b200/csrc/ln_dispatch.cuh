@@ -371,9 +371,8 @@ struct BwdVec {
         constexpr bool kStats = (MODE & lnk::kBwdRecompute) != 0;
         const int S =
             std::min(lnk::split_stages<T, NR, NS, kStats>(a.C, lnk::kMaxSmemPerBlock), S_MAX);
-        static_assert(Warps::kLong || Warps::vc == VC, "column vectors per lane");
         constexpr int NCOL = Warps::cols;
-        status = bwd_run<T, true>(a, lnk::ln_bwd_split_kernel<T, VR, Warps::vc, NR, NCOL, MODE>,
+        status = bwd_run<T, true>(a, lnk::ln_bwd_split_kernel<T, VR, VC, NR, NCOL, MODE>,
                                   32 * (NR + NCOL + 1),
                                   lnk::split_smem<T, NR, NS, kStats>(a.C, S), NR, NR);
     }

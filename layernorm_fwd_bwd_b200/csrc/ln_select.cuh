@@ -224,19 +224,13 @@ template <int MODE> constexpr bool split_takes(int v) {
     return v <= kSplitMaxV &&
            (v >= LN_SPLIT_FROM_V || ((MODE & kBwdDropout) != 0 && (v == 4 || v == 5)));
 }
-// Column-warp vectors per lane for rows of 32 * VR vectors.
-template <int VR> struct SplitVc {
-    static constexpr int value =
-        ((32 * VR + SplitCols<VR>::value - 1) / SplitCols<VR>::value + 31) / 32;
-};
-
 // Calls visitor.template split<VR, VC>() if v == VR and such rows take the
 // split ring at all.
 template <int VR, int MODE, typename Visitor>
 bool split_if(int v, Visitor &visitor) {
     if constexpr (split_takes<MODE>(VR)) {
         if (v == VR) {
-            visitor.template split<VR, SplitVc<VR>::value>();
+            visitor.template split<VR, SplitWarps<VR, MODE>::vc>();
             return true;
         }
     }
@@ -284,7 +278,7 @@ bool visit_bwd_ring(int nvec, Visitor &v) {
         case 3: v.template ring<3, 1>(); return true;
         default: break;
     }
-    if constexpr (V1 >= 4) {
+    if constexpr (V1 >= 4 && !(SplitServes<T, MODE>::value && split_takes<MODE>(4))) {
         if (v1 == 4) { v.template ring<4, 1>(); return true; }
     }
     if constexpr (V1 > 4) {
