@@ -47,14 +47,17 @@
  *     output or with an array the call reads (LN_ERR_ALIAS, checked on the
  *     host before anything is launched).  Inputs may overlap one another.
  *     The accumulating backward reads the outputs it adds to; that is the
- *     same array, not an overlap.
- *   - Any alignment is accepted.  Fully 16-byte-aligned arrays with C * size
- *     a multiple of 16 bytes take the vectorised path; others a scalar path.
+ *     same array, not an overlap.  One exception: dresid_out of
+ *     ln_backward_dropout_residual may be dresid.
+ *   - Any alignment is accepted (the dropout calls: of whole elements).  Fully
+ *     16-byte-aligned arrays with C * size a multiple of 16 bytes take the
+ *     vectorised path, others a scalar path; the dropout calls also take rows
+ *     of other lengths on a vectorised path when the [N * C] arrays start on 16
+ *     bytes.
  *   - Errors are returned as an ln_status value; nothing is launched when
  *     validation fails, and no kernel asserts or traps.
  *   - ln_forward, ln_forward_residual, ln_backward, ln_backward_ex and the
- *     dropout calls
- *     can be captured into a CUDA graph (the backward's workspace then
+ *     dropout calls can be captured into a CUDA graph (the backward's workspace then
  *     becomes graph allocation nodes); make one uncaptured call of the same
  *     shape on the device first, so that one-time set-up (the device's memory
  *     pool, kernel attributes) happens outside the capture.

@@ -31,9 +31,11 @@
 //     bits of dweight/dbias are fixed for a given device model and call, but
 //     may differ between devices with different SM counts.  No float atomics
 //     anywhere.
-// No kernel waits on another block or on a flag: the only cross-kernel
-// dependency is programmatic dependent launch (griddepcontrol), resolved by
-// the hardware when the producing grid completes.
+// No kernel waits on a flag in global memory, and none on another block but the
+// one-cluster dropout backward (ln_ragged.cuh), whose blocks meet at the
+// hardware's cluster barrier; the only cross-kernel dependency is programmatic
+// dependent launch (griddepcontrol), resolved by the hardware when the producing
+// grid completes.
 #pragma once
 
 #include "ln_mask.cuh"

@@ -17,7 +17,10 @@
 // 16-bit type: about 7 integer instructions per element.  With 32 bits per
 // element that doubles, and the elementwise kernel would leave the memory
 // roofline (bf16: about 6 elements per clock and SM at the measured copy
-// bandwidth).  T / 65536 differs from p by at most 2^-17; kept elements are
+// bandwidth).  A 16-byte vector of fp32 is half a group: the fused calls draw a
+// group in both lanes that hold its halves, twice the work per element, for half
+// the elements per byte; ln_dropout gives a thread whole groups and draws each
+// once, and the scalar kernels draw one evaluation per element.  T / 65536 differs from p by at most 2^-17; kept elements are
 // scaled by 65536 / (65536 - T), so the result stays unbiased for the rate
 // actually drawn.
 #pragma once

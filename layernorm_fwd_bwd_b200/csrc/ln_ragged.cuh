@@ -1,6 +1,7 @@
 // ln_ragged.cuh -- the dropout-residual forward and backward for rows of any
-// length (arrays that start on a 16-byte boundary), for narrow rows, and for
-// backward calls of few rows.
+// length (arrays that start on a 16-byte boundary), for narrow rows, for
+// backward calls of few rows, and for backward rows wider than the ring kernels
+// serve.
 //
 // Operation: as ln_forward_dropout_residual and ln_backward_dropout_residual in
 // include/ln.h state; arithmetic as in ln_kernels.cuh, mask from ln_mask.cuh.

@@ -15,9 +15,10 @@
 // Rows wider than the widest variant, and any misaligned call, take the
 // scalar kernels.
 // With dropout: forward blocks of one small tile (ln_dispatch.cuh), the split
-// ring also for 4 and 5 vectors per lane, and the kernels of ln_ragged.cuh for
-// rows that are no whole number of vectors, for narrow rows and for backward
-// calls of few rows.
+// ring also for 4 and 5 vectors per lane and with recomputed statistics, and the
+// kernels of ln_ragged.cuh for rows that are no whole number of vectors, for
+// narrow rows, for backward calls of few rows and for backward rows past the
+// ring; the register-resident backward then serves only 16-bit rows wider still.
 #pragma once
 
 #include "ln_kernels.cuh"
@@ -303,8 +304,8 @@ bool visit_bwd_ring(int nvec, Visitor &v) {
     return false;
 }
 
-// Backward rows wider than the ring covers (more than kRingMaxW * 32 * shared
-// vectors): the register-resident kernel with W = 4, 8 or 16 warps per row
+// Backward rows, without dropout, wider than the ring covers (more than
+// kRingMaxW * 32 * shared vectors): the register-resident kernel with W = 4, 8 or 16 warps per row
 // and 4 vectors per thread.  Calls visitor.template run<V, W, GROUPS>();
 // false when rows are wider still.
 template <typename T, typename Visitor>

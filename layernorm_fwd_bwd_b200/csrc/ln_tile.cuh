@@ -26,7 +26,7 @@
 // The residual variant (MODE & kFwdResidual) copies the tiles of both inputs
 // under the same barrier and forms x = inp + branch in registers; with
 // kFwdDropout, x = inp + dropout(branch), whose mask each lane draws for the
-// vectors it holds (one generator call per 16-byte vector).
+// vectors it holds (one generator call per 16-byte vector, in fp32 half of it used).
 #pragma once
 
 #include "ln_mask.cuh"
